@@ -374,8 +374,9 @@ __global__ void __launch_bounds__(kTkThreads) decode_topk_kernel(DecodeSpec ds,
   __syncthreads();
   float l = 0.0f;
   if (n > 0) {
+    const float ref = kRagged && m == -INFINITY ? 0.0f : m;  // every logit -inf: a sum of 0
 #pragma unroll 8
-    for (int i = tid; i < n; i += kTkThreads) l += __expf(sc[i] - m);
+    for (int i = tid; i < n; i += kTkThreads) l += __expf(sc[i] - ref);
   }
   for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
   if (lane == 0) red[warp] = l;
