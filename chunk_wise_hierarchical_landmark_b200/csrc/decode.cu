@@ -1145,7 +1145,8 @@ __global__ void __launch_bounds__(D) decode_combine_kernel(DecodeSpec ds,
   for (int s = 0; s < ds.Q; ++s) {
     const float *r = r0 + s * stride;
     const float m = r[0];
-    if (m == -INFINITY) continue;
+    // a partial without weight; one of a NaN logit alone has the sum NaN
+    if (m == -INFINITY && (!kRagged || r[1] == 0.0f)) continue;
     const float w = __expf(m - M);
     L += w * r[1];
     o += w * r[2 + threadIdx.x];

@@ -22,6 +22,20 @@ def positive_queries(G, d, dtype, seed):
 
 
 @pytest.mark.parametrize("q8,dtype", FORMS)
+def test_nan_keys_of_the_own_chunk_are_not_lost(q8, dtype):
+    """A NaN among the own chunk's keys reaches out and lse of every head, whether other
+    chunks are attended or not."""
+    G, d, K = 2, 64, 3
+    for n_c in (0, 4):
+        c, *_ = filled(1, 1, d, [n_c * C], q8, dtype, seed=725, max_len=n_c * C + 3)
+        x = randn((1, 1, 3, d), 726, dtype)
+        x[0, 0, 1, 7] = math.nan
+        hb.kv_append(c, x.cuda(), x.abs().nan_to_num(1.0).cuda(), ints([n_c * C]))
+        got = step(c, positive_queries(G, d, dtype, 727), n_c * C + 3, K, debug_checks=True)
+        assert got["out"].isnan().all() and got["lse"].isnan().all()
+
+
+@pytest.mark.parametrize("q8,dtype", FORMS)
 @pytest.mark.parametrize("low", [-1.0])
 def test_every_landmark_banned_in_a_long_cache(q8, dtype, low):
     """More than 8192 completed chunks, every landmark -inf: the lowest chunks fill the
