@@ -188,7 +188,8 @@ __global__ void __launch_bounds__(kThreads) cache_attn_simt_kernel(
       const float x1 = lane + 32 < e.rows ? s.xs[g * kC + lane + 32] : -INFINITY;
       float m = fmaxf(x0, x1);
       for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const float e0 = __expf(x0 - m), e1 = __expf(x1 - m);
+      const float ref = m == -INFINITY ? 0.0f : m;  // every logit -inf: a sum of 0
+      const float e0 = __expf(x0 - ref), e1 = __expf(x1 - ref);
       float l = e0 + e1;
       for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
       s.xs[g * kC + lane] = e0;
@@ -216,7 +217,8 @@ __global__ void __launch_bounds__(kThreads) cache_attn_simt_kernel(
       float o = 0.0f;
 #pragma unroll 8
       for (int j = 0; j < kC; ++j) o = fmaf(s.xs[g * kC + j], s.vs[j * D + col], o);
-      acc[u] = acc[u] * s.so[g] + s.sn[g] * o;
+      // weight 0: no part of its values, also of infinities and NaN (0 times them is NaN)
+      acc[u] = acc[u] * s.so[g] + (s.sn[g] == 0.0f ? 0.0f : s.sn[g] * o);
     }
     __syncthreads();
   }
@@ -449,8 +451,9 @@ __device__ __forceinline__ void own_chunk(const DecodeSpec &ds, const CacheKV &c
       ll += a * rw[1];
       oo += a * rw[2 + e];
     }
-    // one entry of the fusion: logit m + log l, weight 1, output o / l
-    rec[hd * kRec + 2 + e] = oo / ll;
+    // one entry of the fusion: logit m + log l, weight 1, output o / l (every
+    // token's logit -inf: l = 0, the logit -inf, the output of no weight 0)
+    rec[hd * kRec + 2 + e] = ll == 0.0f ? 0.0f : oo / ll;
     if (e == 0) *reinterpret_cast<float2 *>(rec + hd * kRec) = make_float2(mm + __logf(ll), 1.0f);
   }
 }
@@ -903,7 +906,8 @@ __global__ void __launch_bounds__(kWarps * 32) cache_attn_mma_kernel(
 }
 
 // The chunks of a head fused (one CTA per head): out = sum w_c o_c, w the
-// softmax over the selected landmark logits and the own chunk's.  A warp sums
+// softmax over the selected landmark logits and the own chunk's.  A logit of
+// -inf weighs 0; a head that has no other gets out 0, lse -inf.  A warp sums
 // every eighth record, a lane D / 32 columns, all its loads at once.
 constexpr int kCombWarps = 8;
 template <int D>
@@ -949,8 +953,8 @@ __global__ void __launch_bounds__(kCombWarps * 32) cache_combine_kernel(
   float l = e0 + e1;
 #pragma unroll
   for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  const float eown = __expf(wown - m);
-  l += eown;
+  const float eown = wown == -INFINITY ? 0.0f : __expf(wown - m);
+  l += eown;  // at least 1, or 0 where every logit is -inf
   float acc[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = 0.0f;
@@ -968,7 +972,7 @@ __global__ void __launch_bounds__(kCombWarps * 32) cache_combine_kernel(
     float y = eown * own[2 + tid];
 #pragma unroll
     for (int w = 0; w < kCombWarps; ++w) y += wo[w][tid];
-    orow[tid] = __float2bfloat16_rn(y / l);
+    orow[tid] = __float2bfloat16_rn(l == 0.0f ? 0.0f : y / l);
   }
   if (tid == 0) lse[h] = m + __logf(l);
 }

@@ -990,9 +990,10 @@ __global__ void __launch_bounds__(kAttnThreads, HILS_DECODE_MINB) decode_attn_ke
       }
       x0 = lane <= jmax ? x0 : -INFINITY;
       x1 = lane + 32 <= jmax ? x1 : -INFINITY;
-      float m = fmaxf(x0, x1);  // finite: key 0 is always in the chunk
+      float m = fmaxf(x0, x1);  // finite for finite inputs: key 0 is always in the chunk
       for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const float e0 = __expf(x0 - m), e1 = __expf(x1 - m);
+      const float ref = kRagged && m == -INFINITY ? 0.0f : m;  // every logit -inf: a sum of 0
+      const float e0 = __expf(x0 - ref), e1 = __expf(x1 - ref);
       float l = e0 + e1;
       for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
       ps[lane * GB + g] = e0;
@@ -1038,11 +1039,11 @@ __global__ void __launch_bounds__(kAttnThreads, HILS_DECODE_MINB) decode_attn_ke
           }
         }
       }
-      // a head that does not attend the chunk keeps clear of its values, also of
-      // infinities and NaN (0 times them is NaN)
+      // a head that does not attend the chunk, or with a logit of -inf, keeps clear
+      // of its values, also of infinities and NaN (0 times them is NaN)
 #pragma unroll
       for (int g = 0; g < GB; ++g)
-        if (kRagged && !((mask >> g) & 1u)) {
+        if (kRagged && (!((mask >> g) & 1u) || st[g * 4 + 2] == -INFINITY)) {
           (g & 1 ? oa[g / 2].y : oa[g / 2].x) = 0.0f;
           (g & 1 ? ob[g / 2].y : ob[g / 2].x) = 0.0f;
         }
@@ -1151,7 +1152,8 @@ __global__ void __launch_bounds__(D) decode_combine_kernel(DecodeSpec ds,
     L += w * r[1];
     o += w * r[2 + threadIdx.x];
   }
-  out[(size_t)h * D + threadIdx.x] = from_f<T>(o / L);
+  // kRagged: every logit of the head -inf (L = 0) gives out 0, lse -inf
+  out[(size_t)h * D + threadIdx.x] = from_f<T>(kRagged && L == 0.0f ? 0.0f : o / L);
   if (threadIdx.x == 0) lse[h] = M + __logf(L);
 }
 

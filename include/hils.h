@@ -315,6 +315,9 @@ hils_status hils_kv_append(const hils_params *p, const hils_kv_cache *cache, int
  *            batch row) selects nothing: out 0, lse and lse_lmk -inf
  *   outputs  as in hils_decode_fwd; rows with fewer than topk completed
  *            chunks are padded with -1 / -inf
+ *            A chunk whose fusion logit is -inf (a landmark of -inf, an own
+ *            chunk whose token logits all are) weighs 0, whatever its values;
+ *            a head that has no other chunk: out 0, lse -inf
  *   ws       hils_workspace_size(p, HILS_OP_DECODE_CACHE) bytes
  * cache->lmk may be NULL when L <= C.  num_pages * Hkv (times C for fp32
  * pages) must be below 2^31.  An out-of-bounds length counts as 0; a

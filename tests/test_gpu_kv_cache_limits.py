@@ -22,6 +22,70 @@ def positive_queries(G, d, dtype, seed):
 
 
 @pytest.mark.parametrize("q8,dtype", FORMS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_own_chunk_without_a_logit_weighs_nothing(q8, dtype, d):
+    """Keys of -inf in the whole own chunk: its fusion logit is -inf, its values
+    (NaN among them) do not matter and the rest is fused without it, as with keys so
+    low that the weight is 0 in 32 bits."""
+    G, K, n_c, own = 3, 2, 4, 17
+    c, k, v, _ = filled(1, 1, d, [n_c * C], q8, dtype, seed=700 + d, max_len=n_c * C + own)
+    q = positive_queries(G, d, dtype, 701)
+    got = []
+    for low in (-math.inf, -1e4):
+        x, y = torch.full((1, 1, own, d), low, dtype=dtype), randn((1, 1, own, d), 702, dtype)
+        if low == -math.inf:
+            y[0, 0, 3, 5], y[0, 0, 4, 6] = math.inf, math.nan
+        hb.kv_append(c, x.cuda(), y.cuda(), ints([n_c * C]))
+        got.append(step(c, q, n_c * C + own, K, debug_checks=True))
+    for n in got[0]:
+        assert torch.equal(got[0][n], got[1][n]), n
+    assert got[0]["out"].isfinite().all()
+    # nothing but the selected landmarks' logits: the sum of K exponentials
+    want = torch.logsumexp(got[0]["chunk_w"].double(), -1)
+    assert ((got[0]["lse"].double() - want).abs() <= 2.0 ** -20 * (4 + want.abs())).all()
+
+
+@pytest.mark.parametrize("q8,dtype", FORMS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_head_with_nothing_left(q8, dtype, d):
+    """An own chunk of keys of -inf and no other chunk, or only chunks banned by
+    their landmarks: out 0, lse -inf; a sequence beside it is served."""
+    G, K = 2, 3
+    for n_c in (0, 1, 3, 5):
+        N = n_c * C + 9
+        c, *_ = filled(2, 1, d, [n_c * C, N], q8, dtype, seed=710 + n_c, max_len=N)
+        lm = c.lmk.clone()
+        lm[0, :, :n_c] = -math.inf
+        c = c.replace(lmk=lm)
+        x = torch.full((2, 1, 9, d), -math.inf, dtype=dtype).cuda()
+        hb.kv_append(c, x, randn((2, 1, 9, d), 711, dtype).cuda(), ints([n_c * C, 0]), n_new=ints([9, 0]))
+        q = positive_queries(G, d, dtype, 712).repeat(2, 1, 1)
+        got = hb.decode_cache(q, c, ints([N, N]), K, debug_checks=True)
+        assert not got["out"][0].any()
+        assert (got["lse"][0] == -math.inf).all() and (got["lse_lmk"][0] == -math.inf).all()
+        assert (got["chunk_w"][0] == -math.inf).all()
+        assert got["sel_idx"][0].tolist() == [[i if i < n_c else -1 for i in range(K)]] * G
+        assert got["out"][1].isfinite().all() and got["out"][1].any() and got["lse"][1].isfinite().all()
+
+
+@pytest.mark.parametrize("q8,dtype", FORMS)
+def test_values_of_a_banned_chunk_do_not_matter(q8, dtype):
+    """NaN among the values of a chunk whose landmark logit is -inf."""
+    G, d, K, N = 2, 64, 4, 4 * C + 5
+    c, *_ = filled(1, 1, d, [N], q8, dtype, seed=720)
+    q = positive_queries(G, d, dtype, 721)
+    lm = c.lmk.clone()
+    lm[0, 0, 2] = -math.inf
+    c = c.replace(lmk=lm)
+    want = step(c, q, N, K)
+    c.v_pages[int(c.page_table[0, 2]), 0, 7] = math.nan
+    got = step(c, q, N, K)
+    for n in got:
+        assert torch.equal(got[n], want[n]), n
+    assert got["out"].isfinite().all()
+
+
+@pytest.mark.parametrize("q8,dtype", FORMS)
 def test_nan_keys_of_the_own_chunk_are_not_lost(q8, dtype):
     """A NaN among the own chunk's keys reaches out and lse of every head, whether other
     chunks are attended or not."""
@@ -36,7 +100,7 @@ def test_nan_keys_of_the_own_chunk_are_not_lost(q8, dtype):
 
 
 @pytest.mark.parametrize("q8,dtype", FORMS)
-@pytest.mark.parametrize("low", [-1.0])
+@pytest.mark.parametrize("low", [-math.inf, -1.0])
 def test_every_landmark_banned_in_a_long_cache(q8, dtype, low):
     """More than 8192 completed chunks, every landmark -inf: the lowest chunks fill the
     selection with weight 0, lse_lmk is -inf and the own chunk takes all (low:
