@@ -250,9 +250,9 @@ __global__ void __launch_bounds__(kThreads) cache_attn_simt_kernel(
 //   softmax  the 64 logits of a head lie in the eight lanes of equal t
 //   P V      A = 16 dims x 16 keys (two rows interleaved byte by byte), B =
 //            keys x 8 heads, the logits' fragments transposed in registers;
-//            probabilities times 2^15 in fp16 (11 bits: four times finer than
-//            the bf16 output), accumulated in fp32; 1 / l, of the same scaled
-//            probabilities in fp32, takes the factor out again
+//            probabilities times 2^15 in two fp16 parts (22 bits), accumulated
+//            in fp32; 1 / l, of the same scaled probabilities in fp32, takes the
+//            factor out again
 // The order of the 16 keys of a step is free as long as K and V agree: row g
 // of the fragment is key kperm(g), which keeps both the K reads (16 bytes of
 // 8 rows) and the V reads clear of bank conflicts at d = 128.
@@ -787,7 +787,14 @@ __global__ void __launch_bounds__(kWarps * 32) cache_attn_mma_kernel(
       const unsigned char *vbk = ring + (j % kSlots) * Lay::kItem;
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
-        const uint32_t b0 = movm(pack_h2(s[ks][0], s[ks][1])), b1 = movm(pack_h2(s[ks][2], s[ks][3]));
+        uint32_t ph[2], pl[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t top = pack_h2(s[ks][2 * u], s[ks][2 * u + 1]);
+          const float2 r = __half22float2(*reinterpret_cast<const __half2 *>(&top));
+          ph[u] = movm(top);
+          pl[u] = movm(pack_h2(s[ks][2 * u] - r.x, s[ks][2 * u + 1] - r.y));
+        }
         uint32_t w[4][DG / 4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -812,10 +819,12 @@ __global__ void __launch_bounds__(kWarps * 32) cache_attn_mma_kernel(
           uint32_t a0, a1, a2, a3;
           e4m3x4_to_f16x2(x0, a0, a1);
           e4m3x4_to_f16x2(y0, a2, a3);
-          mma_f16(o[2 * e], a0, a1, a2, a3, b0, b1);
+          mma_f16(o[2 * e], a0, a1, a2, a3, ph[0], ph[1]);
+          mma_f16(o[2 * e], a0, a1, a2, a3, pl[0], pl[1]);
           e4m3x4_to_f16x2(x1, a0, a1);
           e4m3x4_to_f16x2(y1, a2, a3);
-          mma_f16(o[2 * e + 1], a0, a1, a2, a3, b0, b1);
+          mma_f16(o[2 * e + 1], a0, a1, a2, a3, ph[0], ph[1]);
+          mma_f16(o[2 * e + 1], a0, a1, a2, a3, pl[0], pl[1]);
         }
       }
       __syncwarp();
