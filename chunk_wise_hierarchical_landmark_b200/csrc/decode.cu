@@ -1146,11 +1146,19 @@ __global__ void __launch_bounds__(D) decode_combine_kernel(DecodeSpec ds,
   for (int s = 0; s < ds.Q; ++s) {
     const float *r = r0 + s * stride;
     const float m = r[0];
-    // a partial without weight; one of a NaN logit alone has the sum NaN
-    if (m == -INFINITY && (!kRagged || r[1] == 0.0f)) continue;
-    const float w = __expf(m - M);
-    L += w * r[1];
-    o += w * r[2 + threadIdx.x];
+    if constexpr (kRagged) {
+      // no branch, so that the loads are all in flight.  A partial without
+      // weight has the sum 0; one of a NaN logit alone has the sum NaN
+      const float l = r[1], x = r[2 + threadIdx.x];
+      const float w = m == -INFINITY && l == 0.0f ? 0.0f : __expf(m - M);
+      L += w * l;
+      o += w * x;
+    } else {
+      if (m == -INFINITY) continue;
+      const float w = __expf(m - M);
+      L += w * r[1];
+      o += w * r[2 + threadIdx.x];
+    }
   }
   // kRagged: every logit of the head -inf (L = 0) gives out 0, lse -inf
   out[(size_t)h * D + threadIdx.x] = from_f<T>(kRagged && L == 0.0f ? 0.0f : o / L);
