@@ -40,7 +40,8 @@ constexpr size_t kDebugWs = 256;
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-hils_status check_params(const hils_params *p) {
+// The bounds of every call.
+hils_status check_shape(const hils_params *p) {
   if (!p) return fail(HILS_ERR_INVALID_ARG, "params is NULL");
   if (p->B < 1 || p->Hq < 1 || p->Hkv < 1 || p->L < 1 || p->d < 1 || p->chunk < 1 ||
       p->topk < 1 || p->M < 1)
@@ -60,6 +61,14 @@ hils_status check_params(const hils_params *p) {
   if (p->L > kMaxL) return fail(HILS_ERR_UNSUPPORTED, "L=%d above %d", p->L, kMaxL);
   if ((int64_t)p->B * p->Hq > (1 << 16) - 1)
     return fail(HILS_ERR_UNSUPPORTED, "B*Hq above 65535");
+  return HILS_OK;
+}
+
+// ... and of the calls that index rows (b, head, token) with 32 bits; those over a
+// cache that grows do not: their L is a capacity.
+hils_status check_params(const hils_params *p) {
+  const hils_status s = check_shape(p);
+  if (s != HILS_OK) return s;
   if ((int64_t)p->B * p->Hq * p->L >= (int64_t)1 << 31)
     return fail(HILS_ERR_UNSUPPORTED, "B*Hq*L must be below 2^31");
   return HILS_OK;
@@ -161,16 +170,16 @@ hils_status check_decode(const hils_params *p) {
 }  // namespace
 
 HILS_API size_t hils_workspace_size(const hils_params *p, int op) {
+  if (op == HILS_OP_DECODE_CACHE) {  // either form of the cache
+    if (check_shape(p) != HILS_OK || check_decode(p) != HILS_OK) return 0;
+    return std::max(hils::decode_workspace_bytes(cache_spec_of(p, false)),
+                    hils::decode_workspace_bytes(cache_spec_of(p, true)));
+  }
   if (check_params(p) != HILS_OK) return 0;
   if (op == HILS_OP_PREFILL) return p->debug_checks ? kDebugWs : 0;
   if (op == HILS_OP_DECODE) {
     if (check_decode(p) != HILS_OK) return 0;
     return hils::decode_workspace_bytes(decode_spec_of(p));
-  }
-  if (op == HILS_OP_DECODE_CACHE) {  // either form of the cache
-    if (check_decode(p) != HILS_OK) return 0;
-    return std::max(hils::decode_workspace_bytes(cache_spec_of(p, false)),
-                    hils::decode_workspace_bytes(cache_spec_of(p, true)));
   }
   return 0;
 }
@@ -380,7 +389,7 @@ HILS_API hils_status hils_kv_append(const hils_params *p, const hils_kv_cache *c
                                     const int32_t *n_new, const hils_rows *q, void *q_out,
                                     int n_rope_pairs, double base, int32_t *seq_lens, void *ws,
                                     size_t ws_bytes, void *stream) {
-  hils_status s = check_params(p);
+  hils_status s = check_shape(p);
   if (s != HILS_OK) return s;
   hils::CacheKV c;
   if ((s = check_cache(p, cache, &c)) != HILS_OK) return s;
@@ -423,7 +432,7 @@ HILS_API hils_status hils_decode_fwd_cache(const hils_params *p, const hils_kv_c
                                            int32_t *sel_idx, float *chunk_w, float *lse_lmk,
                                            void *out, float *lse, void *ws, size_t ws_bytes,
                                            void *stream) {
-  hils_status s = check_params(p);
+  hils_status s = check_shape(p);
   if (s != HILS_OK) return s;
   hils::CacheKV c;
   if ((s = check_cache(p, cache, &c)) != HILS_OK) return s;

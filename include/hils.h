@@ -239,6 +239,8 @@ hils_status hils_decode_fwd_noalloc(const hils_params *p, const void *q, const v
  *       a decode step is read.
  * lmk [B,Hkv,lmk_rows,d] (params dtype) holds the landmark keys, one row per
  * complete chunk; NULL in hils_kv_append leaves them to the caller.
+ * Bounds of the calls over it: L <= 2^24 (a capacity, at most), B * Hq <= 65535
+ * and B * max_pages, num_pages below 2^31, and those named at each call.
  * A sequence may be cut back (a decode step and the next append take the
  * shorter length) to any length >= 1, in the 8-bit form as long as its tails
  * still hold the new length's own chunk, that is, as no later chunk of the
@@ -319,8 +321,8 @@ hils_status hils_kv_append(const hils_params *p, const hils_kv_cache *cache, int
  *            chunk whose token logits all are) weighs 0, whatever its values;
  *            a head that has no other chunk: out 0, lse -inf
  *   ws       hils_workspace_size(p, HILS_OP_DECODE_CACHE) bytes
- * cache->lmk may be NULL when L <= C.  num_pages * Hkv (times C for fp32
- * pages) must be below 2^31.  An out-of-bounds length counts as 0; a
+ * cache->lmk may be NULL when L <= C.  B * Hkv * lmk_rows and num_pages * Hkv
+ * (times C for fp32 pages) must be below 2^31.  An out-of-bounds length counts as 0; a
  * chunk whose table entry lies outside [0, num_pages) is not read (the
  * outputs of the heads that select it are unspecified); with p->debug_checks
  * both return HILS_ERR_DEVICE_CHECK.

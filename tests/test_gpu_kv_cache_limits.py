@@ -136,3 +136,45 @@ def test_every_landmark_banned_in_a_long_cache(q8, dtype, low):
     assert ((got["out"][0].double() - want).abs() <= tol).all()
     lse = -q[0].double().sum(-1) / math.sqrt(d) + math.log(rows)
     assert ((got["lse"][0].double() - lse).abs() <= 2.0 ** -18 * (4 + lse.abs())).all()
+
+
+@pytest.mark.parametrize("q8,dtype", FORMS)
+def test_room_for_a_million_tokens(q8, dtype):
+    """64 sequences of 32 heads with room for 2^20 tokens each (2^31 query rows), a
+    few hundred of them there: the same as with room for those alone, but for
+    the order of the sums of lse_lmk, and in the fp32 8-bit form, whose grid
+    follows the capacity, of the merges of a head's K + 1 = 4 chunks: 4 times
+    two exponentials of 2^-21 and 2^-22 per unit of their argument (at most the
+    range of the logits), in the numerator and in the sum, on both sides."""
+    B, H, Hq, d, K, L = 64, 4, 32, 64, 3, 1 << 20
+    n = [(37 * b) % 450 for b in range(B)]
+    need = 8
+    table = torch.full((B, L // C), -1, dtype=torch.int32)
+    g = torch.Generator().manual_seed(740)
+    table[:, :need] = torch.randperm(B * need, generator=g).view(B, need).to(torch.int32)
+    wide = hb.alloc_kv_cache(B, H, d, L, num_pages=B * need, page_table=table.cuda(), q8=q8, dtype=dtype)
+    tight = hb.alloc_kv_cache(B, H, d, need * C, num_pages=B * need, page_table=table[:, :need].cuda().contiguous(),
+                              q8=q8, dtype=dtype)
+    k, v = randn((B, H, 450, d), 741, dtype).cuda(), randn((B, H, 450, d), 742, dtype).cuda()
+    q = randn((B, Hq, 1, d), 743, dtype).cuda()
+    got = []
+    for c in (wide, tight):
+        lens = hb.kv_append(c, k, v, ints([0] * B), n_new=ints(n))["seq_lens"]
+        r = hb.kv_append(c, k[:, :, :1], v[:, :, :1], lens, q=q, n_rope_pairs=20)
+        assert r["seq_lens"].tolist() == [x + 1 for x in n]
+        got.append(hb.decode_cache(r["q"].view(B, Hq, d), c, r["seq_lens"], K, debug_checks=True))
+    for name in got[0]:
+        a, z = got[0][name], got[1][name]
+        if name != "lse_lmk" and (not q8 or dtype == BF16 or name in ("sel_idx", "chunk_w")):
+            assert torch.equal(a, z), name
+            continue
+        fin = z != -math.inf
+        assert torch.equal(a != -math.inf, fin)
+        if name == "lse_lmk":
+            assert ((a - z).abs()[fin] <= 2.0 ** -19 * (4 + z.abs()[fin])).all()
+            continue
+        w = got[0]["chunk_w"]
+        span = float(w[w != -math.inf].abs().max()) + float(got[0]["lse"].abs().max())
+        tol = 32 * (2.0 ** -21 + 2.0 ** -22 * span)
+        assert tol < 2.0 ** -12
+        assert ((a - z).abs() <= tol * (float(v.abs().max()) if name == "out" else 1.0)).all(), name
