@@ -9,8 +9,9 @@ libhils.so is missing or fails to load, every call raises.
 from __future__ import annotations
 
 import contextlib
-import functools
+import copyreg
 import ctypes
+import functools
 import os
 
 import torch
@@ -345,7 +346,8 @@ class KVCache(_CacheFields):
     The tensors are checked against each other once, here (the C ABI sees
     pointers only); a handle keeps its tensors, whose contents the calls
     change, and its attributes are fixed.  replace() makes a handle with other
-    tensors."""
+    tensors, copy.copy one with the same; a deep copy and a saved one (torch.save)
+    hold tensors of their own.  A subclass may add fields."""
     __slots__ = ()
 
     def __new__(cls, k_pages, v_pages, page_table, lmk=None, k_scale=None, v_scale=None,
@@ -385,14 +387,38 @@ class KVCache(_CacheFields):
         self.B, self.Hkv, self.d, self.q8, self.dtype, self.max_len = B, H, d, q8, dt, mp * 64
         self.device, self._dev = k_pages.device, dev
         self._c = _CacheStruct(HILS_CACHE_Q8 if q8 else HILS_CACHE_PAGED, mp, rows, npg, *ptrs)
-        self.__class__ = cls
-        return self
+        if cls is KVCache:
+            self.__class__ = cls  # a step makes handles: 7 us this way, 10 us filling a sealed one
+            return self
+        handle = object.__new__(cls)  # a subclass may have fields of its own
+        for name in _CacheFields.__slots__:
+            object.__setattr__(handle, name, getattr(self, name))
+        return handle
 
-    def __setattr__(self, name, value):  # _c holds the tensors' pointers
-        raise AttributeError(f"KVCache.{name} is fixed; replace() makes a handle with other tensors")
+    def __setattr__(self, name, value):
+        self._fixed(name)
+        object.__setattr__(self, name, value)
+
+    def __delattr__(self, name):
+        self._fixed(name)
+        object.__delattr__(self, name)
+
+    def _fixed(self, name):  # _c holds the tensors' pointers
+        if name in _CacheFields.__slots__:
+            raise AttributeError(f"KVCache.{name} is fixed; replace() makes a handle with other tensors")
+
+    def _tensors(self):
+        return {n: getattr(self, n) for n in _CacheFields.__slots__[:8]}
+
+    def __reduce__(self):
+        return copyreg.__newobj__, (type(self), *self._tensors().values()), getattr(self, "__dict__", None)
 
     def replace(self, **tensors) -> "KVCache":
-        return KVCache(**{**{n: getattr(self, n) for n in _CacheFields.__slots__[:8]}, **tensors})
+        cls = type(self)
+        handle = cls.__new__(cls, **{**self._tensors(), **tensors})
+        if cls is not KVCache and hasattr(self, "__dict__"):
+            handle.__dict__.update(self.__dict__)
+        return handle
 
 
 def alloc_kv_cache(B, Hkv, d, max_len, num_pages=None, page_table=None, q8=True,
