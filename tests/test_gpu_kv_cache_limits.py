@@ -178,3 +178,19 @@ def test_room_for_a_million_tokens(q8, dtype):
         tol = 32 * (2.0 ** -21 + 2.0 ** -22 * span)
         assert tol < 2.0 ** -12
         assert ((a - z).abs() <= tol * (float(v.abs().max()) if name == "out" else 1.0)).all(), name
+
+
+def test_sizes_past_32_bits_are_refused():
+    """By the library's own errors; their low 32 bits would be good sizes."""
+    c = hb.alloc_kv_cache(1, 2, 64, 256)
+    k, q = randn((1, 2, 3, 64), 750, BF16).cuda(), randn((1, 4, 64), 751, BF16).cuda()
+    before = c.k_tail.clone()
+    for wide in ((1 << 32) + 256, 256 - (1 << 32)):
+        for call in (lambda: hb.kv_append(c, k, k, ints([0]), max_len=wide),
+                     lambda: hb.decode_cache(q, c, ints([3]), 4, max_len=wide)):
+            with pytest.raises(hb.HilsError):
+                call()
+    for wide in ((1 << 32) + 8, 8 - (1 << 32)):
+        with pytest.raises(hb.HilsError):
+            hb.kv_append(c, k, k, ints([0]), n_rope_pairs=wide)
+    assert torch.equal(c.k_tail, before)

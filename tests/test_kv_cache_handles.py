@@ -80,3 +80,12 @@ def test_copies(cls, q8):
             a, b = getattr(c, n), getattr(z, n)
             assert (a is None and b is None) or torch.equal(a.float(), b.float())
             assert a is None or z is s or a.data_ptr() != b.data_ptr()
+
+
+def test_tables_past_32_bits_are_refused():
+    """The library counts table entries in 32 bits (tensors without memory)."""
+    z = dict(device="meta", dtype=torch.bfloat16)
+    pages = torch.empty((4, 2, 64, 64), **z)
+    for shape in ((1, (1 << 32) + 4), (2, 1 << 30)):
+        with pytest.raises(ValueError, match="page_table"):
+            hb.KVCache(pages, pages, torch.empty(shape, device="meta", dtype=torch.int32))
