@@ -558,7 +558,7 @@ def decode_cache(q, cache: KVCache, seq_lens, topk, max_len=None, scale=None,
                                        bool(debug_checks))
     with _on(cache):
         # allocations are half of a small step's host time; with strides they take less
-        K = max(topk, 0)  # a topk out of bounds is refused by the call
+        K = topk if ws_bytes else 1  # sizes without a workspace are refused by the call
         w = torch.empty_strided((B, Hq, K), (Hq * K, K, 1), dtype=torch.float32, device=dev)
         sel = torch.empty_like(w, dtype=torch.int32)
         lse = torch.empty_strided((B, Hq), (Hq, 1), dtype=torch.float32, device=dev)

@@ -194,3 +194,16 @@ def test_sizes_past_32_bits_are_refused():
         with pytest.raises(hb.HilsError):
             hb.kv_append(c, k, k, ints([0]), n_rope_pairs=wide)
     assert torch.equal(c.k_tail, before)
+
+
+@pytest.mark.parametrize("topk", [65, 1 << 26, (1 << 32) + 8, 8 - (1 << 32)])
+def test_a_refused_topk_allocates_nothing_of_its_size(topk):
+    c = hb.alloc_kv_cache(1, 2, 64, 256)
+    q = randn((1, 4, 64), 752, BF16).cuda()
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    base = torch.cuda.memory_allocated()
+    with pytest.raises(hb.HilsError) as e:
+        hb.decode_cache(q, c, ints([3]), topk)
+    assert e.value.status in (1, 2)
+    assert torch.cuda.max_memory_allocated() - base < 1 << 20
