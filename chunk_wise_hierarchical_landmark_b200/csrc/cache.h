@@ -43,12 +43,12 @@ cudaError_t kv_append(const AppendSpec &as, bool bf16, const CacheKV &c, const R
                       const RowsIn &v, const RowsIn &q, void *q_out, const HopeParams &hp,
                       uint32_t *err, cudaStream_t st, int *launches);
 
-// A union entry resolved (cache_select or decode_union writes it), two uint4:
-// the block of the chunk, or one of the negative codes; the mask of the heads
-// that attend it; the two scales (fp32 bits); and, a byte per head, the place of
-// the chunk in the head's selection.
+// A union entry of a completed chunk resolved (cache_select or decode_union
+// writes it), two uint4: the block of the chunk, or kEntNoPage; the mask of the
+// heads that attend it; the two scales (fp32 bits); and, a byte per head, the
+// place of the chunk in the head's selection.  The own chunk, the union's last, has
+// none: its attention needs no selection (u_count counts it all the same).
 constexpr int kEntNoPage = -1;  // the page lies outside the pool
-constexpr int kEntOwn = -2;     // the own chunk (the last entry), read from the tail
 
 constexpr int kCacheWarps = 4;       // warps of a tensor-core attention CTA
 constexpr int kCacheMaxPer = 128;    // most union entries per warp, where parts are fixed

@@ -578,13 +578,9 @@ __global__ void __launch_bounds__(kSelThreads, kPer > 8 || D > 0 ? 4 : 8) cache_
     }
   }
   if (rank == 0 && tid == 0) {
-    if (own >= 0) {  // every head attends its own chunk
-      if (ent) {
-        ent[2 * (u0 + total)] = make_uint4((uint32_t)kEntOwn, (1u << G) - 1u, 0u, 0u);
-      } else {
-        u_c[u0 + total] = own;
-        u_mask[u0 + total] = (1u << G) - 1u;
-      }
+    if (own >= 0 && !ent) {  // every head attends its own chunk
+      u_c[u0 + total] = own;
+      u_mask[u0 + total] = (1u << G) - 1u;
     }
     u_count[bk] = own >= 0 ? total + 1 : 0;
     if (bk == 0 && next) *next = 0;

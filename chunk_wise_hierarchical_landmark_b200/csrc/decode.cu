@@ -715,24 +715,20 @@ __global__ void __launch_bounds__(256) decode_union_kernel(DecodeSpec ds,
     u_count[bk] = total;
   }
   if (kRagged && ent) {
-    // the entries resolved to blocks and scales
+    // the entries but the last, the own chunk's, resolved to blocks and scales
     __syncthreads();
-    for (int i = tid; i < total; i += blockDim.x) {
-      const int c = uc[i];
-      uint4 e = make_uint4((uint32_t)kEntOwn, um[i], 0u, 0u);
-      if (c != own) {
-        const long long page = cache.table[(size_t)b * cache.max_pages + c];
-        if (page >= 0 && page < cache.num_pages) {
-          const size_t blk = (size_t)page * ds.Hkv + hkv;
-          e.x = (uint32_t)blk;
-          if (cache.q8) {
-            e.z = __float_as_uint(cache.k_scale[blk]);
-            e.w = __float_as_uint(cache.v_scale[blk]);
-          }
-        } else {
-          e.x = (uint32_t)kEntNoPage;
-          report(err, DEV_BAD_INDEX);
+    for (int i = tid; i < total - 1; i += blockDim.x) {
+      uint4 e = make_uint4((uint32_t)kEntNoPage, um[i], 0u, 0u);
+      const long long page = cache.table[(size_t)b * cache.max_pages + uc[i]];
+      if (page >= 0 && page < cache.num_pages) {
+        const size_t blk = (size_t)page * ds.Hkv + hkv;
+        e.x = (uint32_t)blk;
+        if (cache.q8) {
+          e.z = __float_as_uint(cache.k_scale[blk]);
+          e.w = __float_as_uint(cache.v_scale[blk]);
         }
+      } else {
+        report(err, DEV_BAD_INDEX);
       }
       ent[2 * ((size_t)bk * cap + i)] = e;
     }

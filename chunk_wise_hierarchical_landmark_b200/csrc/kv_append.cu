@@ -552,7 +552,7 @@ cudaError_t kv_append(const AppendSpec &as, bool bf16, const CacheKV &c, const R
     return cudaGetLastError();
   }
   // T tokens from any position touch at most this many chunks
-  const unsigned nx = as.T == 1 ? 1u : (unsigned)((as.T - 1) / kC + 2);
+  const unsigned nx = (unsigned)((as.T - 1) / kC + 2);
   const dim3 grid(nx, (unsigned)(2 * as.Hkv + (q.p ? as.Hq : 0)), (unsigned)as.B);
 #define HILS_APPEND(T, DD)                                                                     \
   do {                                                                                         \
