@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kThreads) cache_attn_simt_kernel(
           const float mn = fmaxf(s.M[g], lg);
           const float w = __expf(lg - mn);
           s.so[g] = __expf(s.M[g] - mn);
-          s.sn[g] = w / l * e.sv;
+          s.sn[g] = w / l;
           s.L[g] = s.L[g] * s.so[g] + w;
           s.M[g] = mn;
         }
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kThreads) cache_attn_simt_kernel(
 #pragma unroll 8
       for (int j = 0; j < kC; ++j) o = fmaf(s.xs[g * kC + j], s.vs[j * D + col], o);
       // weight 0: no part of its values, also of infinities and NaN (0 times them is NaN)
-      acc[u] = acc[u] * s.so[g] + (s.sn[g] == 0.0f ? 0.0f : s.sn[g] * o);
+      acc[u] = acc[u] * s.so[g] + (s.sn[g] == 0.0f ? 0.0f : s.sn[g] * (o * e.sv));
     }
     __syncthreads();
   }
@@ -899,11 +899,13 @@ __global__ void __launch_bounds__(kWarps * 32) cache_attn_mma_kernel(
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (!att[h]) continue;
-      const float inv = (Q8 ? sv : 1.0f) / l[h];
+      // the scale apart: its product with 1 / l (down to 2^-21) would be subnormal
+      // for the least scales and lose its bits
+      const float inv = 1.0f / l[h], f = Q8 ? sv : 1.0f;
 #pragma unroll
       for (int mt = 0; mt < MT; mt += 2)
         *reinterpret_cast<float4 *>(rec[h] + (Q8 ? 2 * mt : 64 * (mt / 4) + 2 * (mt % 4))) =
-            make_float4(o[mt][h] * inv, o[mt][2 + h] * inv, o[mt + 1][h] * inv, o[mt + 1][2 + h] * inv);
+            make_float4(o[mt][h] * inv * f, o[mt][2 + h] * inv * f, o[mt + 1][h] * inv * f, o[mt + 1][2 + h] * inv * f);
     }
   }
   if (!ok && lane == 0) {

@@ -68,3 +68,42 @@ def test_probabilities_over_8_bit_blocks_keep_22_bits(d):
     assert float(ref["out"].abs().min(-1).values.max()) < 2.0 ** -6  # every head has a sum near 0
     tol = 2 * (8 * 2.0 ** -24 * 0.25 + 2.0 ** -21 + 2.0 ** -22 + 2.0 ** -22) + 130 * 2.0 ** -24
     assert ((got - ref["out"]).abs() <= tol + 2.0 ** -8 * ref["out"].abs()).all()
+
+
+def scaled_twice(v, q, N, K, dtype):
+    """The decode of a batch whose values are v, and v times 2^-119 with its out times 2^119."""
+    B, H, _, d = v.shape
+    g = torch.Generator().manual_seed(831)
+    k = torch.randn((B, H, N, d), generator=g).to(dtype).cuda()
+    got = []
+    for e in (0, -119):
+        c = hb.alloc_kv_cache(B, H, d, N, q8=True, dtype=dtype)
+        hb.kv_append(c, k, (v.double() * 2.0 ** e).to(dtype), ints([0] * B))
+        if e:
+            assert 2.0 ** -126 <= float(c.v_scale[c.v_scale > 0].min()) <= 2.0 ** -123
+        got.append(hb.decode_cache(q, c, ints([N] * B), K, max_len=N))
+    for n in ("sel_idx", "chunk_w", "lse", "lse_lmk"):
+        assert torch.equal(got[0][n], got[1][n]), n
+    return got[0]["out"].double(), got[1]["out"].double() * 2.0 ** 119
+
+
+@pytest.mark.parametrize("dtype", [BF16, torch.float32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("coherent", [False, True])
+def test_values_near_the_least_scales(d, dtype, coherent):
+    """Values times 2^-119 (scales near 2^-126) give the outputs times 2^-119: a power of two
+    moves no bit but where intermediate results become subnormal.  What that
+    leaves, times 2^119, is 2^-31 for a sum; it may carry a rounding that lay at its
+    border to the next step: in fp32 at most 8 of them (the merges of K + 1 = 5
+    chunks, two records, a division), each a step, 2^-23, of the largest value; in
+    bf16 one more, 2^-7 of out, or 2^-14 where out is subnormal."""
+    B, H, G, K, N = 2, 2, 4, 4, 9 * C + 7
+    g = torch.Generator().manual_seed(830)
+    v = torch.randn((B, H, N, d), generator=g)
+    if coherent:
+        v = 3.75 + 0.25 * v.tanh()  # the products of a chunk add up
+    q = (torch.randn((B, H * G, d), generator=g) / 8).to(dtype).cuda()
+    a, z = scaled_twice(v.to(dtype).cuda(), q, N, K, dtype)
+    tol = 8 * 2.0 ** -23 * float(v.abs().max())
+    tol = tol if dtype != BF16 else 2.0 ** -7 * a.abs() + 2.0 ** -14 + tol
+    assert ((a - z).abs() <= tol).all(), float((a - z).abs().max())
