@@ -15,9 +15,9 @@
 // decode.cu's chunk attention.
 //
 // Bound by the bytes of the attended blocks.  Measured (16 sequences of 512K,
-// 32 / 8 heads, d = 128, top 64, 8 bits): 92 us for 531 MB, 5.8 TB/s, 89 % of a
-// plain copy; a quarter of the batch takes 33 us, so beyond some 12 us of start
-// and end the rate is the copy's.  The tensor pipe is at 14 %: the G <= 8 heads
+// 32 / 8 heads, d = 128, top 64, 8 bits): 93 us for 531 MB, 5.7 TB/s, 88 % of a
+// plain copy; a quarter of the batch takes 32 us, so beyond some 12 us of start
+// and end the rate is the copy's.  The tensor pipe is at 21 %: the G <= 8 heads
 // of a KV head fill the 8 columns of m16n8k16, where a tcgen05 tile of 128 rows
 // would be filled to a sixteenth by heads, or need the 64 keys of two chunks
 // that other heads attend.
@@ -252,7 +252,9 @@ __global__ void __launch_bounds__(kThreads) cache_attn_simt_kernel(
 //            keys x 8 heads, the logits' fragments transposed in registers;
 //            probabilities times 2^15 in two fp16 parts (22 bits), accumulated
 //            in fp32; 1 / l, of the same scaled probabilities in fp32, takes the
-//            factor out again
+//            factor out again.  (One part, 11 bits, is off by up to 1.2e-4 of
+//            the values' mean magnitude, two by 1e-8; its step of 16 x 512K
+//            takes 166.2 instead of 167.1 us.)
 // The order of the 16 keys of a step is free as long as K and V agree: row g
 // of the fragment is key kperm(g), which keeps both the K reads (16 bytes of
 // 8 rows) and the V reads clear of bank conflicts at d = 128.

@@ -591,7 +591,11 @@ __global__ void __launch_bounds__(kSelThreads, kPer > 8 || D > 0 ? 4 : 8) cache_
 
 // Few enough landmarks per KV head for its cluster to score them itself, which
 // saves a launch (a step of 1000 tokens 17.9 -> 16.9 us on the device, 45 ->
-// 41 us with the host's part).
+// 41 us with the host's part).  This and the scores per thread below go by ds.n_c,
+// the bound that the call gives for its sequences; their lengths are on the device.
+// Room for more costs a step of 1000 tokens 14.4 -> 15.6 us (128K), 17.0 us
+// (512K) and, by the radix select past 8192 chunks, 19.7 us (1M), a batch of
+// lengths up to 128K 88.5 -> 96.0 us (512K) and 100.6 us (1M).
 bool cache_select_scores(const DecodeSpec &ds, bool bf16) { return bf16 && ds.n_c <= 2 * kSelThreads; }
 
 cudaError_t cache_scores(const DecodeSpec &ds, const void *q, const void *lmk, float *scores,

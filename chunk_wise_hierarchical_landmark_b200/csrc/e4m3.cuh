@@ -1,7 +1,9 @@
 // The 8-bit cache format: e4m3 codes (sign, 4 exponent bits, 3 mantissa bits;
 // largest value 448, no infinities) with one power-of-two scale per block of
-// 64 tokens of a KV head.  value = code * scale, exact in bf16 and fp32: a
-// power of two only moves the exponent, so the one rounding is the code's.
+// 64 tokens of a KV head.  value = code * scale, exact in fp32 (and in bf16 for
+// scales from 2^-124 on; below, the smallest codes' values are under its least
+// subnormal): a power of two only moves the exponent, so the one rounding is the
+// code's.
 #pragma once
 
 #include <cuda_fp16.h>
