@@ -446,21 +446,23 @@ def alloc_kv_cache(B, Hkv, d, max_len, num_pages=None, page_table=None, q8=True,
     return KVCache(*pages, page_table, lmk, *(more if q8 else ()))
 
 
-# A serving loop calls with the same sizes again and again: the parameter block
-# of a call (read only) and its workspace bytes are kept by its arguments.
-_params = functools.lru_cache(maxsize=1024)(make_params)
-
-
-@functools.lru_cache(maxsize=1024)
-def _decode_cache_params(*args):
-    p = make_params(*args)
-    return p, lib().hils_workspace_size(p, HILS_OP_DECODE_CACHE)
-
-
 def _c_int(x):
     """x as the library sees it: past 32 bits still out of its bounds (ctypes would
     pass the low bits)."""
     return min(max(x, -1), (1 << 31) - 1)
+
+
+# A serving loop calls with the same sizes again and again: the parameter block
+# of a call (read only) and its workspace bytes are kept by its arguments.
+@functools.lru_cache(maxsize=1024)
+def _params(B, Hq, Hkv, L, d, topk, *rest):
+    return make_params(B, Hq, Hkv, _c_int(L), d, _c_int(topk), *rest)
+
+
+@functools.lru_cache(maxsize=1024)
+def _decode_cache_params(*args):
+    p = _params(*args)
+    return p, lib().hils_workspace_size(p, HILS_OP_DECODE_CACHE)
 
 
 def _on(cache):
@@ -517,7 +519,7 @@ def kv_append(cache: KVCache, k, v, pos, n_new=None, q=None, n_rope_pairs=0, bas
     pos_p = _lens(pos, cache, "pos")
     n_p = None if n_new is None else _lens(n_new, cache, "n_new")
     lens_p = None if seq_lens is None else _lens(seq_lens, cache, "seq_lens")
-    p = _params(B, Hq, H, _c_int(cache.max_len if max_len is None else int(max_len)), d, 1, 64, 64, 1.0,
+    p = _params(B, Hq, H, cache.max_len if max_len is None else int(max_len), d, 1, 64, 64, 1.0,
                 cache.dtype, bool(debug_checks))
     with _on(cache):
         if rq is not None and q_out is None:
@@ -527,8 +529,9 @@ def kv_append(cache: KVCache, k, v, pos, n_new=None, q=None, n_rope_pairs=0, bas
             lens_p = seq_lens.data_ptr()
         ws = torch.empty(256, dtype=torch.uint8, device=cache.device) if debug_checks else None
         _check(lib().hils_kv_append(p, cache._c, T, rk, rv, pos_p, n_p, rq,
-                                    None if q_out is None else q_out.data_ptr(), _c_int(n_rope_pairs),
-                                    base, lens_p, *_ws_args(ws), _current_stream(cache)))
+                                    None if q_out is None else q_out.data_ptr(),
+                                    n_rope_pairs if -1 < n_rope_pairs < 1 << 31 else -1, base,
+                                    lens_p, *_ws_args(ws), _current_stream(cache)))
     return dict(q=q_out, seq_lens=seq_lens)
 
 
@@ -552,8 +555,8 @@ def decode_cache(q, cache: KVCache, seq_lens, topk, max_len=None, scale=None,
         raise ValueError(f"q must be a contiguous [{B}, Hq, {d}] {dt} tensor on {dev}")
     _lens(seq_lens, cache, "seq_lens")
     Hq = q.shape[1]
-    topk = _c_int(int(topk))
-    p, ws_bytes = _decode_cache_params(B, Hq, cache.Hkv, _c_int(cache.max_len if max_len is None else int(max_len)),
+    topk = int(topk)
+    p, ws_bytes = _decode_cache_params(B, Hq, cache.Hkv, cache.max_len if max_len is None else int(max_len),
                                        d, topk, 64, 64, None if scale is None else float(scale), dt,
                                        bool(debug_checks))
     with _on(cache):
